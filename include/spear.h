@@ -275,6 +275,13 @@ typedef struct spear_kv_cache {
  *   block_table : int32 [table_rows][max_pages], rows table_stride apart;
  *                 entry j is the page of tokens [j page_size, (j + 1) page_size)
  *   seq_lens    : int32 [table_rows], cached tokens, the call's new ones included.
+ *   refused     : NULL, or the word moves + 1 of the rows' spear_kv_pool: with it
+ *                 spear_kv_append writes nothing (and reports
+ *                 SPEAR_ERR_INVALID_ARG) after a spear_kv_reserve that was
+ *                 refused.  The lengths do not count the new tokens then, and
+ *                 their rows would replace the sequences' last cached ones, in
+ *                 pages that a fork may share.  The attention calls take no
+ *                 notice of it.
  * Entries past a row's last page are not read.  A row, length or page number
  * out of range is reported as SPEAR_ERR_INVALID_ARG through
  * spear_get_device_status: the length is clamped, a missing page reads as
@@ -286,6 +293,7 @@ typedef struct spear_kv_seqs {
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* seq_ids;
+  const int32_t* refused;
 } spear_kv_seqs;
 
 /*
@@ -293,7 +301,9 @@ typedef struct spear_kv_seqs {
  * [num_seqs + 1]): sequence b's new tokens are the rows [starts[b],
  * starts[b + 1]) of k_new and v_new, its last ones: row starts[b + 1] - 1 goes
  * to position seq_lens - 1.  Element (token, head, d) of k_new is at token
- * k_token_stride + head k_head_stride + d (multiples of 8 elements).
+ * k_token_stride + head k_head_stride + d (multiples of 8 elements).  After
+ * spear_kv_reserve pass seqs->refused: the call cannot tell otherwise that the
+ * lengths did not grow.
  */
 spear_status spear_kv_append(const spear_kv_cache* cache, const spear_kv_seqs* seqs, const int32_t* starts,
                              int num_tokens, const uint16_t* k_new, int64_t k_token_stride, int64_t k_head_stride,
@@ -359,6 +369,8 @@ spear_status spear_attn_prefill(const spear_kv_cache* cache, const spear_kv_seqs
  *   block_table : int32 [max_seqs][max_pages], -1 past a row's last page
  *   moves       : int32 [2 + 3 num_pages], page copies of the last call:
  *                 [0] their number, then from [2] pairs (source, destination);
+ *                 [1] bit 0: the last spear_kv_reserve was refused (zeroed once
+ *                 before the first call; only spear_kv_reserve changes the bit);
  *                 the rest is scratch
  * The calls run on the device in stream order and need no answer on the host.
  * Free pages are taken in ascending order.  A call with an entry that is out

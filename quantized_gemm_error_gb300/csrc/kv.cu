@@ -25,12 +25,17 @@ __device__ unsigned g_kv_status;
 // a copy of 2 Hkv D elements a token, bound by memory.
 constexpr int kAppendThreads = 256, kAppendUnroll = 4;
 
+// Bits of a pool's moves[1].
+constexpr int kReserveRefused = 1;     // by the last reserve; append reads it
+constexpr int kForkRefused = 2;        // by the take kernel, for the fork's second kernel
+
 struct AppendArgs {
   KvView c;
   SeqView s;
   const uint16_t *k_new, *v_new;
   int64_t kt, kh, vt, vh;              // token and head strides of the new rows
   const int32_t* starts;               // [n + 1]: sequence b's tokens are [starts[b], starts[b + 1])
+  const int32_t* refused;              // the word that says whether the lengths count the new tokens (NULL: they do)
   int tokens, vecs;                    // vecs: 16-byte pieces of one head's row
 };
 
@@ -46,7 +51,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     }
     int64_t off = -1;
     const int end = a.starts[lo + 1];
-    if (a.starts[lo] <= t && t < end && end <= a.tokens) {
+    if (a.refused && (*a.refused & kReserveRefused)) {
+      record_status(&g_kv_status, DEV_ERR_INVALID);
+    } else if (a.starts[lo] <= t && t < end && end <= a.tokens) {
       const int row = seq_row(a.s, lo, &g_kv_status);
       const int len = seq_len(a.s, a.c, row, &g_kv_status);
       const int pos = len - (end - t);
@@ -96,9 +103,9 @@ PoolView pool_view(const spear_kv_pool& p) {
           FastDiv::of((uint32_t)p.page_size)};
 }
 
-// moves: [0] count, [1] nonzero when the call was refused, then `count` pairs
-// (source page, destination page) from [2]; [2 + 2 num_pages ..] is scratch of
-// num_pages words (the free list of reserve and fork, compact's renaming).
+// moves: [0] count, [1] what was refused, then `count` pairs (source page,
+// destination page) from [2]; [2 + 2 num_pages ..] is scratch of num_pages
+// words (the free list of reserve and fork, compact's renaming).
 __device__ __forceinline__ int32_t* pool_scratch(const PoolView& p) { return p.moves + 2 + 2 * (int64_t)p.num_pages; }
 
 // Exclusive prefix sum of v over the block; *total gets the sum.
@@ -133,7 +140,7 @@ struct Need {
 // One block: checks every entry, finds the total of new pages and takes the
 // lowest free ones in the entries' order.  Nothing is changed when an entry is
 // invalid or the pool is too small; that is recorded, and moves[1] says so to
-// the kernel that follows.
+// the fork's second kernel, or to the appends that follow a reserve.
 template <bool FORK>
 __global__ void __launch_bounds__(kPoolThreads)
 pool_take_kernel(PoolView p, const int32_t* rows, const int32_t* arg, int n) {
@@ -220,7 +227,8 @@ pool_take_kernel(PoolView p, const int32_t* rows, const int32_t* arg, int n) {
   const bool refused = s_bad || found < total;
   if (tid == 0) {
     p.moves[0] = 0;
-    p.moves[1] = refused;
+    if (FORK) p.moves[1] = (p.moves[1] & kReserveRefused) | (refused ? kForkRefused : 0);
+    else p.moves[1] = refused ? kReserveRefused : 0;
     if (refused) record_status(&g_kv_status, DEV_ERR_INVALID);
   }
   if (refused) return;
@@ -322,7 +330,7 @@ __global__ void __launch_bounds__(kPoolThreads) pool_compact_plan_kernel(PoolVie
   }
   if (tid == 0) {
     p.moves[0] = highs;
-    p.moves[1] = L;
+    rename[0] = L;                                  // page 0 is never renamed: with a live page, L > 0
   }
 }
 
@@ -394,7 +402,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 fork_apply_kernel(const __grid_constant__ CopyArgs a, PoolView p, const int32_t* parents, const int32_t* children,
                   int n) {
   enter();
-  if (p.moves[1]) return;                                     // refused
+  if (p.moves[1] & kForkRefused) return;
   if (blockIdx.y == 0) {
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
       const int32_t* from = p.table + (int64_t)parents[i] * p.max_pages;
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const __gri
   enter();
   if (blockIdx.y == 0) {
     const int32_t* rename = pool_scratch(p);
-    const int L = p.moves[1];
+    const int L = rename[0];
     for (int i = blockIdx.x; i < p.max_seqs; i += gridDim.x) {
       int32_t* row = p.table + (int64_t)i * p.max_pages;
       for (int j = threadIdx.x; j < p.max_pages; j += kCopyThreads) {
@@ -475,7 +483,7 @@ int copy_grid(const CopyArgs& a, int ncaches, long long other, const DeviceInfo&
 int launch_kv_append(const spear_kv_cache& c, const spear_kv_seqs& s, const int32_t* starts, int tokens,
                      const uint16_t* k_new, int64_t kt, int64_t kh, const uint16_t* v_new, int64_t vt, int64_t vh,
                      cudaStream_t st) {
-  AppendArgs a{kv_view(c), seq_view(s), k_new, v_new, kt, kh, vt, vh, starts, tokens, c.head_dim / 8};
+  AppendArgs a{kv_view(c), seq_view(s), k_new, v_new, kt, kh, vt, vh, starts, s.refused, tokens, c.head_dim / 8};
   return launch_dependent(kv_append_kernel, dim3(tokens), kAppendThreads, 0, st, "kv_append launch", a);
 }
 

@@ -7,7 +7,9 @@ cache per block, one page pool for all of them, and workspaces.  A step takes
 any mix of sequences and new tokens (one token each: the decode kernels; more:
 the prefill kernels), and sequences can be forked, finished and the pool
 compacted between steps.  Everything runs in stream order on the GPU; no call
-reads an answer back.
+reads an answer back.  A call that the pool would refuse is refused on the host
+before anything is launched (PoolFull where pages are short): the server counts
+along, so the pool's bookkeeping goes through its methods only.
 
 Norms, rotary embeddings and the feed-forward half are not part of it: a block
 maps its input rows to the o projection's output rows.
@@ -42,6 +44,81 @@ class AttentionBlock:
         return self.k.N // self.head_dim
 
 
+class PoolFull(RuntimeError):
+    """A step or fork needs more pages than are free.  Nothing was launched: it can be tried again after finish()."""
+
+
+class PageCount:
+    """The lengths and the number of free pages of a page pool, counted on the host: what spear_kv_reserve,
+    spear_kv_fork and spear_kv_free will find on the device, and the calls that they would refuse.
+
+    A row's pages are a list of runs [pages, rows that share them]; a run with more than one row is of whole pages."""
+
+    def __init__(self, num_pages: int, page_size: int, max_seqs: int, max_pages: int):
+        self.page_size, self.max_pages, self.free_pages = page_size, max_pages, num_pages
+        self.lens = [0] * max_seqs
+        self.runs: List[list] = [[] for _ in range(max_seqs)]
+
+    def _check_rows(self, rows: Sequence[int], once: bool) -> None:
+        if any(not 0 <= r < len(self.lens) for r in rows):
+            raise ValueError(f"rows must be in [0, {len(self.lens)}), got {list(rows)}")
+        if once and len(set(rows)) != len(rows):
+            raise ValueError(f"a row is listed twice: {list(rows)}")
+
+    def _take(self, pages: int) -> None:
+        if pages > self.free_pages:
+            raise PoolFull(f"{pages} pages needed, {self.free_pages} free")
+        self.free_pages -= pages
+
+    def reserve(self, rows: Sequence[int], counts: Sequence[int]) -> None:
+        self._check_rows(rows, True)
+        if len(counts) != len(rows) or any(n < 0 for n in counts):
+            raise ValueError(f"counts must be one number >= 0 for each of {len(rows)} rows, got {list(counts)}")
+        need = []
+        for r, n in zip(rows, counts):
+            want = self.lens[r] + n
+            if want > min(self.max_pages * self.page_size, 0x7fffffff - self.page_size):
+                raise ValueError(f"row {r} would hold {want} tokens, a row has {self.max_pages} pages of {self.page_size}")
+            need.append(-(-want // self.page_size) - -(-self.lens[r] // self.page_size))
+        self._take(sum(need))
+        for r, n, pages in zip(rows, counts, need):
+            runs = self.runs[r]
+            if pages and runs and runs[-1][1] == 1:
+                runs[-1][0] += pages
+            elif pages:
+                runs.append([pages, 1])
+            self.lens[r] += n
+
+    def fork(self, parents: Sequence[int], children: Sequence[int]) -> None:
+        self._check_rows(children, True)
+        self._check_rows(parents, False)
+        if len(parents) != len(children):
+            raise ValueError(f"{len(parents)} parents, {len(children)} children")
+        if any(self.lens[c] for c in children) or set(parents) & set(children):
+            raise ValueError(f"children must be empty rows and no parents, got {list(children)}")
+        self._take(sum(self.lens[p] % self.page_size > 0 for p in parents))
+        for p, c in zip(parents, children):
+            part = self.lens[p] % self.page_size > 0         # the last page, which no other row holds
+            runs = self.runs[p]
+            if part and runs[-1][0] > 1:
+                runs[-1][0] -= 1
+                runs.append([1, 1])
+            shared = runs[:-1] if part else runs
+            for run in shared:
+                run[1] += 1
+            self.runs[c] = list(shared) + ([[1, 1]] if part else [])
+            self.lens[c] = self.lens[p]
+
+    def free(self, rows: Sequence[int]) -> None:
+        self._check_rows(rows, False)
+        for r in rows:
+            for run in self.runs[r]:
+                run[1] -= 1
+                if not run[1]:
+                    self.free_pages += run[0]
+            self.runs[r], self.lens[r] = [], 0
+
+
 class PagedServer:
     """Blocks, their caches and the sequences in flight (rows 0 .. max_seqs - 1 of the page pool)."""
 
@@ -51,6 +128,7 @@ class PagedServer:
         self.device, self.stream = torch.device(device), stream
         self.caches = [spear.new_kv_cache(num_pages, page_size, b.kv_heads, b.head_dim, device) for b in self.blocks]
         self.pool = spear.PagePool(num_pages, page_size, max_seqs, max_pages, device)
+        self.count = PageCount(num_pages, page_size, max_seqs, max_pages)
 
     def _rows(self, rows: Sequence[int]) -> torch.Tensor:
         return torch.tensor(list(rows), dtype=torch.int32, device=self.device)
@@ -68,6 +146,7 @@ class PagedServer:
             starts.append(starts[-1] + n)
         if starts[-1] != x.shape[0]:
             raise ValueError(f"x has {x.shape[0]} rows, counts add up to {starts[-1]}")
+        self.count.reserve(rows, counts)
         ids, dev_starts = self._rows(rows), self._rows(starts)
         table, lens = self.pool.block_table, self.pool.seq_lens
         one_each = all(n == 1 for n in counts)
@@ -78,7 +157,7 @@ class PagedServer:
             q = self._linear(b.q, x).view(T, b.q_heads, D)
             k = self._linear(b.k, x).view(T, b.kv_heads, D)
             v = self._linear(b.v, x).view(T, b.kv_heads, D)
-            spear.spear_kv_append(cache, k, v, table, lens, dev_starts, seq_ids=ids, stream=self.stream)
+            spear.spear_kv_append(cache, k, v, table, lens, dev_starts, seq_ids=ids, pool=self.pool, stream=self.stream)
             kw = dict(seq_ids=ids, window=b.window, sinks=b.sinks, stream=self.stream)
             if one_each:
                 a = spear.spear_attn_decode(q, cache, table, lens, **kw)
@@ -89,9 +168,12 @@ class PagedServer:
 
     def fork(self, parents: Sequence[int], children: Sequence[int]) -> None:
         """Each empty row children[i] continues from a copy of parents[i]."""
+        self.count.fork(parents, children)
         spear.spear_kv_fork(self.pool, self.caches, self._rows(parents), self._rows(children), stream=self.stream)
 
     def finish(self, rows: Sequence[int]) -> None:
+        """Empties the rows (those that are empty already stay so)."""
+        self.count.free(rows)
         spear.spear_kv_free(self.pool, self._rows(rows), stream=self.stream)
 
     def compact(self) -> None:
@@ -99,4 +181,4 @@ class PagedServer:
         spear.spear_kv_compact(self.pool, self.caches, stream=self.stream)
 
 
-__all__ = ["AttentionBlock", "PagedServer"]
+__all__ = ["AttentionBlock", "PageCount", "PagedServer", "PoolFull"]

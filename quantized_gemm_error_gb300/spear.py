@@ -67,7 +67,7 @@ class _Cache(ctypes.Structure):
 class _Seqs(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int), ("max_pages", ctypes.c_int), ("table_rows", ctypes.c_int),
                 ("table_stride", ctypes.c_int64), ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
-                ("seq_ids", ctypes.c_void_p)]
+                ("seq_ids", ctypes.c_void_p), ("refused", ctypes.c_void_p)]
 
 
 class _Attn(ctypes.Structure):
@@ -442,7 +442,8 @@ class PagePool:
         self.seq_lens = self.state[num_pages:num_pages + max_seqs]
         self.block_table = self.state[num_pages + max_seqs:].view(max_seqs, max_pages)
         self.block_table.fill_(-1)
-        # page moves of the last fork or compact: [0] their number, pairs (source, destination) from [2]
+        # page moves of the last fork or compact: [0] their number, pairs (source, destination) from [2]; [1] is odd
+        # while the last reserve was refused
         self.moves = torch.zeros(2 + 3 * num_pages, dtype=torch.int32, device=device)
         self.device = self.state.device
         self.c = _Pool(num_pages, page_size, max_seqs, max_pages, self.refs.data_ptr(), self.seq_lens.data_ptr(),
@@ -516,15 +517,19 @@ def _attn(q, cache, scale, window, sinks, out, lse):
 
 def spear_kv_append(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, block_table: torch.Tensor,
                     seq_lens: torch.Tensor, starts: torch.Tensor, *, seq_ids: Optional[torch.Tensor] = None,
-                    stream=None) -> None:
+                    pool: Optional[PagePool] = None, stream=None) -> None:
     """Writes the new tokens' rows k_new, v_new [tokens][kv_heads][head_dim] into their pages: rows [starts[b],
-    starts[b + 1]) are the last tokens of sequence b, whose length seq_lens counts them already."""
+    starts[b + 1]) are the last tokens of sequence b, whose length seq_lens counts them already.  Pass the `pool`
+    whose spear_kv_reserve made room for them: where it was refused the call then writes nothing and reports
+    SPEAR_ERR_INVALID_ARG (without it the rows would replace the sequences' last cached ones)."""
     T, _, kt, kh = _token_rows(k_new, "k_new", cache.dtype, cache.num_kv_heads, cache.head_dim)
     Tv, _, vt, vh = _token_rows(v_new, "v_new", cache.dtype, cache.num_kv_heads, cache.head_dim)
     if T != Tv:
         raise ValueError(f"k_new has {T} tokens, v_new {Tv}")
     p_starts, n = _i32(starts, "starts"), starts.shape[0] - 1
     s = _seqs(block_table, seq_lens, seq_ids, n)
+    if pool is not None:
+        s.refused = pool.c.moves + 4
     _check(load().spear_kv_append(cache.ref, ctypes.byref(s), p_starts, T, k_new.data_ptr(), kt, kh,
                                   v_new.data_ptr(), vt, vh, _raw_stream(stream)), "spear_kv_append")
 
