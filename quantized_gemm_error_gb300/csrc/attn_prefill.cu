@@ -481,7 +481,10 @@ struct Loader {
     uint32_t nslot = 0, phase = 0;                  // slots and their use
     uint32_t late = 0, late_bar = 0;                // such a tile and its barrier; 0: none
     int late_piece = 0, late_keys = 0;
-    const auto finish = [&] {                       // the pieces this lane copied: no barrier needed
+    // Every lane has waited for its own copies of the tile; a lane scans pieces
+    // that others copied (heads of 128), so the warp meets first.
+    const auto finish = [&] {
+      __syncwarp();
       scan(late, late_piece, late_keys);
       hand_on(late_bar);
       late = 0;
