@@ -16,6 +16,7 @@ maps its input rows to the o projection's output rows.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
 
@@ -120,22 +121,41 @@ class PageCount:
 
 
 class PagedServer:
-    """Blocks, their caches and the sequences in flight (rows 0 .. max_seqs - 1 of the page pool)."""
+    """Blocks, their caches and the sequences in flight (rows 0 .. max_seqs - 1 of the page pool).
+
+    With a `stream` the server's work runs there and its buffers belong to it.  Each call first waits (on the GPU) for
+    the work of the caller's current stream, which in turn waits for the call's before it goes on, so inputs and
+    results are used on the caller's stream as with any other call."""
 
     def __init__(self, blocks: Sequence[AttentionBlock], num_pages: int, page_size: int, max_seqs: int, max_pages: int,
                  device, stream: Optional[torch.cuda.Stream] = None):
         self.blocks: List[AttentionBlock] = list(blocks)
         self.device, self.stream = torch.device(device), stream
-        self.caches = [spear.new_kv_cache(num_pages, page_size, b.kv_heads, b.head_dim, device) for b in self.blocks]
-        self.pool = spear.PagePool(num_pages, page_size, max_seqs, max_pages, device)
+        with self._on_stream():
+            self.caches = [spear.new_kv_cache(num_pages, page_size, b.kv_heads, b.head_dim, device) for b in self.blocks]
+            self.pool = spear.PagePool(num_pages, page_size, max_seqs, max_pages, device)
         self.count = PageCount(num_pages, page_size, max_seqs, max_pages)
+
+    @contextlib.contextmanager
+    def _on_stream(self):
+        """The server's stream as the current one, after the caller's work so far and before what it does next."""
+        if self.stream is None:
+            yield
+            return
+        here = torch.cuda.current_stream(self.device)
+        self.stream.wait_stream(here)
+        try:
+            with torch.cuda.stream(self.stream):
+                yield
+        finally:
+            here.wait_stream(self.stream)
 
     def _rows(self, rows: Sequence[int]) -> torch.Tensor:
         return torch.tensor(list(rows), dtype=torch.int32, device=self.device)
 
     def _linear(self, layer: spear.W4Layer, x: torch.Tensor) -> torch.Tensor:
         call = spear.spear_linear_decode if x.shape[0] <= 64 else spear.spear_linear_prefill
-        return call(layer, x, stream=self.stream)
+        return call(layer, x)
 
     def step(self, x: torch.Tensor, rows: Sequence[int], counts: Sequence[int]) -> List[torch.Tensor]:
         """Runs x (bf16 [sum(counts)][width]: counts[i] new tokens of sequence rows[i], in order) through every block on
@@ -147,18 +167,28 @@ class PagedServer:
         if starts[-1] != x.shape[0]:
             raise ValueError(f"x has {x.shape[0]} rows, counts add up to {starts[-1]}")
         self.count.reserve(rows, counts)
+        here = torch.cuda.current_stream(self.device)
+        with self._on_stream():
+            outs = self._step(x, rows, counts, starts)
+        if self.stream is not None:                          # used on both streams: not reused before either is done
+            x.record_stream(self.stream)
+            for y in outs:
+                y.record_stream(here)
+        return outs
+
+    def _step(self, x: torch.Tensor, rows: Sequence[int], counts: Sequence[int], starts: List[int]) -> List[torch.Tensor]:
         ids, dev_starts = self._rows(rows), self._rows(starts)
         table, lens = self.pool.block_table, self.pool.seq_lens
         one_each = all(n == 1 for n in counts)
-        spear.spear_kv_reserve(self.pool, ids, self._rows(counts), stream=self.stream)
+        spear.spear_kv_reserve(self.pool, ids, self._rows(counts))
         outs = []
         for b, cache in zip(self.blocks, self.caches):
             T, D = x.shape[0], b.head_dim
             q = self._linear(b.q, x).view(T, b.q_heads, D)
             k = self._linear(b.k, x).view(T, b.kv_heads, D)
             v = self._linear(b.v, x).view(T, b.kv_heads, D)
-            spear.spear_kv_append(cache, k, v, table, lens, dev_starts, seq_ids=ids, pool=self.pool, stream=self.stream)
-            kw = dict(seq_ids=ids, window=b.window, sinks=b.sinks, stream=self.stream)
+            spear.spear_kv_append(cache, k, v, table, lens, dev_starts, seq_ids=ids, pool=self.pool)
+            kw = dict(seq_ids=ids, window=b.window, sinks=b.sinks)
             if one_each:
                 a = spear.spear_attn_decode(q, cache, table, lens, **kw)
             else:
@@ -169,16 +199,19 @@ class PagedServer:
     def fork(self, parents: Sequence[int], children: Sequence[int]) -> None:
         """Each empty row children[i] continues from a copy of parents[i]."""
         self.count.fork(parents, children)
-        spear.spear_kv_fork(self.pool, self.caches, self._rows(parents), self._rows(children), stream=self.stream)
+        with self._on_stream():
+            spear.spear_kv_fork(self.pool, self.caches, self._rows(parents), self._rows(children))
 
     def finish(self, rows: Sequence[int]) -> None:
         """Empties the rows (those that are empty already stay so)."""
         self.count.free(rows)
-        spear.spear_kv_free(self.pool, self._rows(rows), stream=self.stream)
+        with self._on_stream():
+            spear.spear_kv_free(self.pool, self._rows(rows))
 
     def compact(self) -> None:
         """Moves the live pages to the front of the pool."""
-        spear.spear_kv_compact(self.pool, self.caches, stream=self.stream)
+        with self._on_stream():
+            spear.spear_kv_compact(self.pool, self.caches)
 
 
 __all__ = ["AttentionBlock", "PageCount", "PagedServer", "PoolFull"]
