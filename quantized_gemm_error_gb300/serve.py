@@ -150,8 +150,10 @@ class PagedServer:
         finally:
             here.wait_stream(self.stream)
 
-    def _rows(self, rows: Sequence[int]) -> torch.Tensor:
-        return torch.tensor(list(rows), dtype=torch.int32, device=self.device)
+    def _rows(self, *lists: Sequence[int]) -> List[torch.Tensor]:
+        """The lists as int32 tensors on the device: one copy from pinned memory, which nothing waits for."""
+        flat = torch.tensor([i for x in lists for i in x], dtype=torch.int32).pin_memory()
+        return list(flat.to(self.device, non_blocking=True).split([len(x) for x in lists]))
 
     def _linear(self, layer: spear.W4Layer, x: torch.Tensor) -> torch.Tensor:
         call = spear.spear_linear_decode if x.shape[0] <= 64 else spear.spear_linear_prefill
@@ -177,10 +179,10 @@ class PagedServer:
         return outs
 
     def _step(self, x: torch.Tensor, rows: Sequence[int], counts: Sequence[int], starts: List[int]) -> List[torch.Tensor]:
-        ids, dev_starts = self._rows(rows), self._rows(starts)
+        ids, new, dev_starts = self._rows(rows, counts, starts)
         table, lens = self.pool.block_table, self.pool.seq_lens
         one_each = all(n == 1 for n in counts)
-        spear.spear_kv_reserve(self.pool, ids, self._rows(counts))
+        spear.spear_kv_reserve(self.pool, ids, new)
         outs = []
         for b, cache in zip(self.blocks, self.caches):
             T, D = x.shape[0], b.head_dim
@@ -200,13 +202,13 @@ class PagedServer:
         """Each empty row children[i] continues from a copy of parents[i]."""
         self.count.fork(parents, children)
         with self._on_stream():
-            spear.spear_kv_fork(self.pool, self.caches, self._rows(parents), self._rows(children))
+            spear.spear_kv_fork(self.pool, self.caches, *self._rows(parents, children))
 
     def finish(self, rows: Sequence[int]) -> None:
         """Empties the rows (those that are empty already stay so)."""
         self.count.free(rows)
         with self._on_stream():
-            spear.spear_kv_free(self.pool, self._rows(rows))
+            spear.spear_kv_free(self.pool, *self._rows(rows))
 
     def compact(self) -> None:
         """Moves the live pages to the front of the pool."""

@@ -77,3 +77,51 @@ def test_a_refused_step_leaves_the_streams_as_they_were():
     assert torch.cuda.current_stream() == here
     torch.cuda.synchronize()
     assert spear.spear_get_device_status() == 0
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_no_call_waits_for_the_gpu(side):
+    """Synchronising calls raise meanwhile, and with a long kernel ahead on the stream all calls return before it ends."""
+    from quantized_gemm_error_gb300 import spear
+    from quantized_gemm_error_gb300.serve import PagedServer
+    s = PagedServer(_blocks(), 200, 16, 8, 40, "cuda", torch.cuda.Stream() if side else None)
+    x = torch.ones(80, 512, dtype=BF16, device="cuda")
+    s.step(x[:40], [0, 7], [39, 1])                          # (what a first call sets up)
+    s.step(x[:2], [0, 7], [1, 1])
+    s.fork([0], [1])
+    s.finish([1, 7])
+    s.compact()
+    torch.cuda.synchronize()
+    begun = torch.cuda.Event()
+    torch.cuda.set_sync_debug_mode("error")
+    try:
+        torch.cuda._sleep(400_000_000)                       # 0.2 s
+        begun.record()
+        s.step(x, [2, 3], [70, 10])
+        s.step(x[:2], [2, 3], [1, 1])
+        s.fork([2], [4])
+        s.finish([3])
+        s.compact()
+        s.step(x[:2], [2, 4], [1, 1])
+        waited = begun.query()
+    finally:
+        torch.cuda.set_sync_debug_mode("default")
+    assert not waited
+    torch.cuda.synchronize()
+    assert spear.spear_get_device_status() == 0
+    assert s.pool.seq_lens.tolist() == s.count.lens
+
+
+def test_empty_calls():
+    from quantized_gemm_error_gb300 import spear
+    from quantized_gemm_error_gb300.serve import PagedServer
+    s = PagedServer(_blocks(), 20, 16, 4, 8, "cuda")
+    x = torch.ones(3, 512, dtype=BF16, device="cuda")
+    s.step(x, [0, 1], [3, 0])
+    s.finish([])
+    s.fork([], [])
+    assert [tuple(y.shape) for y in s.step(x[:0], [0], [0])] == [(0, 512)] * 2
+    assert [tuple(y.shape) for y in s.step(x[:0], [], [])] == [(0, 512)] * 2
+    torch.cuda.synchronize()
+    assert spear.spear_get_device_status() == 0
+    assert s.pool.seq_lens.tolist() == [3, 0, 0, 0]
