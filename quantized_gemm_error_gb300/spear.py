@@ -167,6 +167,19 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(_raw_stream(stream))
 
 
+def _made_on(stream, make, *args, **kw) -> torch.Tensor:
+    """make(*args, **kw), a tensor of the stream that a call runs on: memory of the current stream's could still be in use
+    there by work that is queued.  It may be used on the current stream as well (once that waits for the call)."""
+    if stream is None or _raw_stream(stream) == _raw_stream(None):
+        return make(*args, **kw)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                           torch.cuda.ExternalStream(_raw_stream(stream))):
+        t = make(*args, **kw)
+    t.record_stream(here)
+    return t
+
+
 @dataclass
 class W4Layer:
     """A packed layer plus its compensator (all tensors on the same CUDA device)."""
@@ -251,9 +264,9 @@ def spear_pack_w4(W: torch.Tensor, group_size: int, symmetric: bool, *, out=None
     N, K = W.shape
     qb, sb, zb = spear_pack_w4_sizes(N, K, group_size, symmetric)
     if out is None:
-        q = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
-        s = torch.empty((N, K // group_size), dtype=torch.float16, device=W.device)
-        z = None if symmetric else torch.empty((N, zb // N), dtype=torch.uint8, device=W.device)
+        make = lambda n, dtype: _made_on(stream, torch.empty, (N, n), dtype=dtype, device=W.device)
+        q, s = make(K // 2, torch.uint8), make(K // group_size, torch.float16)
+        z = None if symmetric else make(zb // N, torch.uint8)
     else:
         q, s, z = out
     _check(load().spear_pack_w4(_ptr(W), N, K, group_size, int(symmetric), _ptr(q), _ptr(s), _ptr(z),
@@ -300,9 +313,7 @@ def _default_workspace(kind: str, nbytes: int, device, stream, zero: bool) -> to
     key = (kind, idx, _raw_stream(stream))
     ws = _default_ws.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=torch.device("cuda", idx))
-        if isinstance(stream, torch.cuda.Stream):
-            ws.record_stream(stream)                  # freed (when replaced) only after that stream's work
+        ws = _made_on(stream, torch.empty, max(int(nbytes), 256), dtype=torch.uint8, device=torch.device("cuda", idx))
         if zero:
             spear_workspace_init(ws, stream)          # on the stream the calls use
         _default_ws[key] = ws
@@ -336,10 +347,11 @@ def _check_io(layer: W4Layer, x: torch.Tensor, y: Optional[torch.Tensor], out_dt
                              f"{tuple(y.shape)}")
 
 
-def _out(y, M, N, out_dtype, device):
+def _out(y, M, N, out_dtype, device, stream):
     if y is not None:
         return y
-    return torch.empty((M, N), dtype=torch.float32 if out_dtype == OUT_F32 else torch.bfloat16, device=device)
+    return _made_on(stream, torch.empty, (M, N), dtype=torch.float32 if out_dtype == OUT_F32 else torch.bfloat16,
+                    device=device)
 
 
 def spear_linear_decode(layer: W4Layer, x: torch.Tensor, *, y=None, out_dtype: int = OUT_BF16,
@@ -349,7 +361,7 @@ def spear_linear_decode(layer: W4Layer, x: torch.Tensor, *, y=None, out_dtype: i
     and stream (made once, zeroed, then reused; see reset_default_workspaces)."""
     _check_io(layer, x, y, out_dtype)
     M = x.shape[0]
-    y = _out(y, M, layer.N, out_dtype, x.device)
+    y = _out(y, M, layer.N, out_dtype, x.device, stream)
     if workspace is None:
         workspace = _default_workspace("decode", spear_decode_workspace_bytes(layer, M), x.device, stream, True)
     L = layer.c_struct()
@@ -376,7 +388,7 @@ def spear_linear_prefill(layer: W4Layer, x: torch.Tensor, *, y=None, out_dtype: 
     """Same layer for large M on the tcgen05 tensor-core path."""
     _check_io(layer, x, y, out_dtype)
     M = x.shape[0]
-    y = _out(y, M, layer.N, out_dtype, x.device)
+    y = _out(y, M, layer.N, out_dtype, x.device, stream)
     if workspace is None:
         workspace = _default_workspace("prefill", spear_prefill_workspace_bytes(layer, M, mode), x.device, stream,
                                        False)
@@ -496,11 +508,11 @@ def _token_rows(t: torch.Tensor, name: str, dtype, heads: Optional[int], D: int)
     return T, H, st if T > 1 else 0, sh if H > 1 else 0
 
 
-def _attn(q, cache, scale, window, sinks, out, lse):
+def _attn(q, cache, scale, window, sinks, out, lse, stream):
     D = cache.head_dim
     T, H, st, sh = _token_rows(q, "q", cache.dtype, None, D)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _made_on(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
     elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous() or not out.is_cuda:
         raise ValueError(f"out must be a contiguous {q.dtype} {tuple(q.shape)} CUDA tensor, got {out.dtype} "
                          f"{tuple(out.shape)}")
@@ -547,7 +559,7 @@ def spear_attn_decode(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor
                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of one new token of each sequence, q [seqs][q_heads][head_dim], over its cached keys (its own among
     them); scale defaults to head_dim ** -0.5.  `lse`, when given, receives the rows' log sums (fp32)."""
-    out, a = _attn(q, cache, scale, window, sinks, out, lse)
+    out, a = _attn(q, cache, scale, window, sinks, out, lse, stream)
     s = _seqs(block_table, seq_lens, seq_ids, q.shape[0])
     if workspace is None:
         workspace = cache._workspace("attn_decode", (s.num_seqs, a.num_q_heads), spear_attn_decode_workspace_bytes, True,
@@ -571,7 +583,7 @@ def spear_attn_prefill(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Causal attention of a ragged batch of new tokens, q [tokens][q_heads][head_dim], rows [starts[b],
     starts[b + 1]) the last tokens of sequence b; their K and V rows are in the cache already."""
-    out, a = _attn(q, cache, scale, window, sinks, out, lse)
+    out, a = _attn(q, cache, scale, window, sinks, out, lse, stream)
     p_starts, n = _i32(starts, "starts"), starts.shape[0] - 1
     s = _seqs(block_table, seq_lens, seq_ids, n)
     T = out.shape[0]
