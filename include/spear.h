@@ -322,7 +322,8 @@ spear_status spear_kv_append(const spear_kv_cache* cache, const spear_kv_seqs* s
  * and lse = -inf.  A key that a token does not see has no effect on it,
  * whatever it holds (infinities and NaN included).  Scores, maxima, sums and
  * accumulators are fp32; p is rounded to the call's 16-bit type for the
- * product with V.  out [tokens][num_q_heads][head_dim] is contiguous, lse
+ * product with V (in fp16 with an absolute error below 2^-33 of the row's
+ * largest p where it is smaller than 2^-22 of it).  out [tokens][num_q_heads][head_dim] is contiguous, lse
  * fp32 [tokens][num_q_heads].
  */
 typedef struct spear_attn {

@@ -41,6 +41,14 @@ constexpr int kKept = 1024;                         // sequences whose rows and 
 constexpr int kRingBytes = 192 * 1024;
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 constexpr int kMaxHeads = 16;                       // query heads of an item
+// P is taken times 2^kLift: in fp16 a probability is normal down to 2^-28 of
+// its row's largest so (19 nats; unlifted 2^-14, and below 2^-25 it would be 0,
+// which shows where the largest one's value is near 0, as a sink's is).  l and
+// o carry the factor, so it cancels; lse takes it out of l.  bf16 has fp32's range.
+template <bool F16>
+constexpr float kLift = F16 ? 14.0f : 0.0f;
+template <bool F16>
+__device__ __forceinline__ float log2_sum(float l) { return log2f(l * (F16 ? 0x1p-14f : 1.0f)); }
 
 struct DecArgs {
   KvView c;
@@ -150,7 +158,7 @@ __device__ __forceinline__ void store_row(const DecArgs& a, int64_t row, int d, 
   const float i = 1.0f / l;
   *reinterpret_cast<uint2*>(a.out + row * D + d) =
       make_uint2(pack_elem2<F16>(o.x * i, o.y * i), pack_elem2<F16>(o.z * i, o.w * i));
-  if (a.lse && d == 0) a.lse[row] = (m + log2f(l)) * kLn2;
+  if (a.lse && d == 0) a.lse[row] = (m + log2_sum<F16>(l)) * kLn2;
 }
 // A sequence that sees no key: zeros.
 template <int D>
@@ -395,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             o[n][t][3] *= f1;
           }
         }
-        const float z0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], z1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+        const float z0 = m[n][0] == -INFINITY ? 0.0f : m[n][0] - kLift<F16>;
+        const float z1 = m[n][1] == -INFINITY ? 0.0f : m[n][1] - kLift<F16>;
         const float p0 = ex2(x[0] - z0), p1 = ex2(x[1] - z1), p2 = ex2(x[2] - z0), p3 = ex2(x[3] - z1);
         l[n][0] += p0 + p2;
         l[n][1] += p1 + p3;
@@ -446,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
               for (int e = 0; e < 2; ++e)
                 if (n * 8 + c2 + e < heads)
                   a.lse[(int64_t)use.b * a.q_heads + hq + n * 8 + c2 + e] =
-                      (m[n][e] + log2f(l[n][e])) * kLn2;
+                      (m[n][e] + log2_sum<F16>(l[n][e])) * kLn2;
             }
           }
         } else {

@@ -12,8 +12,8 @@
 // exponentials are taken:
 //   warps 0-3, 4-7   softmax of tile 0 / 1, one row a thread: S from tensor
 //                    memory, P back into its place (16 bits), O rescaled only
-//                    when a row maximum grew by more than 2^15 (the result is
-//                    the same for any m; P stays below 2^15)
+//                    when a row maximum grew by more than 2^kSlack (the result
+//                    is the same for any m; P stays below 2^15)
 //   warps 8, 11      issue the MMAs of tile 0 / 1: S = Q K^T (both from shared
 //                    memory), O += P V (P from tensor memory, V as stored,
 //                    MN-major)
@@ -65,7 +65,21 @@ constexpr uint64_t kLandNs = 2000000000ull;         // limit of the waits for a 
 // log2 growth of a row maximum that is let pass: P stays below 2^15, which fp16
 // holds.  With 8 a row that sees four sinks first is rescaled once more: windowed
 // prompts 174 against 172 us, 8192 tokens 419 against 414.
-constexpr float kSlack = 15.0f;
+//
+// In fp16 the 15 powers of two are shared: P is taken times 2^kLift, so that a
+// probability is normal down to 2^-22 of its row's largest and rounded with an
+// error of 2^-33 of it below (unlifted 2^-14 and 2^-25, which shows where the
+// largest one's value is near 0, as a sink's is).  l and o carry the factor, so
+// it cancels; lse takes it out of l.  A slack of 7 costs 1 % with windowed
+// prompts, nothing with causal ones as long as scores spread over a few nats, and 5
+// to 14 % where they spread over tens; 10 would cost 3 to 7 % there, 4 4 to 10 %
+// everywhere.
+template <bool F16>
+constexpr float kSlack = F16 ? 7.0f : 15.0f;
+template <bool F16>
+constexpr float kLift = F16 ? 8.0f : 0.0f;
+template <bool F16>
+__device__ __forceinline__ float log2_sum(float l) { return log2f(l * (F16 ? 0x1p-8f : 1.0f)); }
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 
 struct PreArgs {
@@ -896,7 +910,7 @@ __device__ __forceinline__ void softmax_role(const PreArgs& a, Shared& sh, int q
     // which arrives on `bar`.
     const auto before = [&](float top, bool filled, const uint64_t& bar, uint32_t parity) {
       top *= a.scale_log2;
-      if (!__any_sync(~0u, top > m + kSlack)) return true;
+      if (!__any_sync(~0u, top > m + kSlack<F16>)) return true;
       const float mn = fmaxf(m, top);
       const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
       m = mn;
@@ -933,7 +947,7 @@ __device__ __forceinline__ void softmax_role(const PreArgs& a, Shared& sh, int q
           if (!(vis >> e & 1)) s[x][e] = 0xff800000u;
       }
     };
-    const auto base_of = [&] { return m == -INFINITY ? 0.0f : m; };
+    const auto base_of = [&] { return m == -INFINITY ? 0.0f : m - kLift<F16>; };
     float top;
     if constexpr (kSplit<D>) {
       // Each half has its own scores: while one is worked on, the tensor cores
@@ -1047,7 +1061,7 @@ __device__ __forceinline__ void softmax_role(const PreArgs& a, Shared& sh, int q
         part[(int64_t)kRows * D + r] = m;
         part[(int64_t)kRows * (D + 1) + r] = l;
       } else if (a.lse) {
-        a.lse[row] = pos < 0 ? -INFINITY : (m + log2f(l)) * kLn2;
+        a.lse[row] = pos < 0 ? -INFINITY : (m + log2_sum<F16>(l)) * kLn2;
       }
     }
   }
@@ -1255,7 +1269,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) attn_prefill_join_kernel(co
   const float inv = pos < 0 ? 0.0f : 1.0f / l;
   *reinterpret_cast<uint2*>(a.out + row * D + 4 * x) =
       make_uint2(pack_elem2<F16>(o.x * inv, o.y * inv), pack_elem2<F16>(o.z * inv, o.w * inv));
-  if (a.lse && x == 0) a.lse[row] = pos < 0 ? -INFINITY : (mx + log2f(l)) * kLn2;
+  if (a.lse && x == 0) a.lse[row] = pos < 0 ? -INFINITY : (mx + log2_sum<F16>(l)) * kLn2;
 }
 
 int encode(CUtensorMap* m, const spear_kv_cache& c, const uint16_t* base, int rank, const cuuint64_t* dims,
