@@ -13,7 +13,7 @@
 //   warps 0-3, 4-7   softmax of tile 0 / 1, one row a thread: S from tensor
 //                    memory, P back into its place (16 bits), O rescaled only
 //                    when a row maximum grew by more than 2^kSlack (the result
-//                    is the same for any m; P stays below 2^15)
+//                    is the same for any m)
 //   warps 8, 11      issue the MMAs of tile 0 / 1: S = Q K^T (both from shared
 //                    memory), O += P V (P from tensor memory, V as stored,
 //                    MN-major)
@@ -62,24 +62,26 @@ constexpr int kGroups = 2048;                       // entries of the prefix ove
 constexpr int kKept = 4096;                         // sequences whose lengths are kept in shared memory meanwhile
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 constexpr uint64_t kLandNs = 2000000000ull;         // limit of the waits for a block's own copies and MMAs, which end by themselves
-// log2 growth of a row maximum that is let pass: P stays below 2^15, which fp16
-// holds.  With 8 a row that sees four sinks first is rescaled once more: windowed
+// log2 growth of a row maximum that is let pass: P's largest values are then up
+// to 2^15 apart.  With 8 a row that sees four sinks first is rescaled once more: windowed
 // prompts 174 against 172 us, 8192 tokens 419 against 414.
 //
-// In fp16 the 15 powers of two are shared: P is taken times 2^kLift, so that a
-// probability is normal down to 2^-22 of its row's largest and rounded with an
-// error of 2^-33 of it below (unlifted 2^-14 and 2^-25, which shows where the
-// largest one's value is near 0, as a sink's is).  l and o carry the factor, so
-// it cancels; lse takes it out of l.  A slack of 7 costs 1 % with windowed
+// P is taken times 2^kLift; l and o carry the factor, so it cancels, and lse
+// takes it out of l.  bf16: 2^-15, so that P stays below 1 and o no larger than
+// the sum of the row's |v| (bf16 has fp32's range, below as above).  fp16: 2^8,
+// so that P stays below 2^15, which fp16 holds, and a probability is normal down
+// to 2^-22 of its row's largest and rounded with an error of 2^-33 of it below
+// (unlifted 2^-14 and 2^-25, which shows where the largest one's value is near
+// 0, as a sink's is).  In fp16 a slack of 7 costs 1 % with windowed
 // prompts, nothing with causal ones as long as scores spread over a few nats, and 5
 // to 14 % where they spread over tens; 10 would cost 3 to 7 % there, 4 4 to 10 %
 // everywhere.
 template <bool F16>
 constexpr float kSlack = F16 ? 7.0f : 15.0f;
 template <bool F16>
-constexpr float kLift = F16 ? 8.0f : 0.0f;
+constexpr float kLift = F16 ? 8.0f : -15.0f;
 template <bool F16>
-__device__ __forceinline__ float log2_sum(float l) { return log2f(l * (F16 ? 0x1p-8f : 1.0f)); }
+__device__ __forceinline__ float log2_sum(float l) { return log2f(l * (F16 ? 0x1p-8f : 0x1p15f)); }
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 
 struct PreArgs {
