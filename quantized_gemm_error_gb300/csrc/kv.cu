@@ -42,7 +42,10 @@ struct AppendArgs {
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
   enter();
   __shared__ int64_t s_off;
+  __shared__ int s_refused;
   const int t = blockIdx.x;
+  // beside the search of thread 0 (in it: 42.1 against 39.4 us for 248 MB)
+  if (threadIdx.x == 32) s_refused = a.refused ? *a.refused & kReserveRefused : 0;
   if (threadIdx.x == 0) {
     int lo = 0, hi = a.s.n;            // last b with starts[b] <= t
     while (hi - lo > 1) {
@@ -51,9 +54,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     }
     int64_t off = -1;
     const int end = a.starts[lo + 1];
-    if (a.refused && (*a.refused & kReserveRefused)) {
-      record_status(&g_kv_status, DEV_ERR_INVALID);
-    } else if (a.starts[lo] <= t && t < end && end <= a.tokens) {
+    if (a.starts[lo] <= t && t < end && end <= a.tokens) {
       const int row = seq_row(a.s, lo, &g_kv_status);
       const int len = seq_len(a.s, a.c, row, &g_kv_status);
       const int pos = len - (end - t);
@@ -66,6 +67,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
   }
   __syncthreads();
   const int64_t off = s_off;
+  if (s_refused) {
+    if (threadIdx.x == 0) record_status(&g_kv_status, DEV_ERR_INVALID);
+    return;
+  }
   if (off < 0) return;
   const int n = a.c.heads * a.vecs;
   for (int i0 = threadIdx.x; i0 < 2 * n; i0 += kAppendUnroll * kAppendThreads) {
