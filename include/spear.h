@@ -374,10 +374,10 @@ spear_status spear_attn_prefill(const spear_kv_cache* cache, const spear_kv_seqs
  *                 before the first call; only spear_kv_reserve changes the bit);
  *                 the rest is scratch
  * The calls run on the device in stream order and need no answer on the host.
- * Free pages are taken in ascending order.  A call with an entry that is out
- * of range or listed twice, or that needs more pages than are free (or than
- * a row holds), changes nothing and reports SPEAR_ERR_INVALID_ARG through
- * spear_get_device_status.  max_seqs <= 262144.
+ * Free pages are taken in ascending order.  A spear_kv_reserve or
+ * spear_kv_fork with an entry that is out of range or listed twice, or that
+ * needs more pages than are free (or than a row holds), changes nothing and
+ * reports SPEAR_ERR_INVALID_ARG through spear_get_device_status.  max_seqs <= 262144.
  */
 typedef struct spear_kv_pool {
   int num_pages, page_size, max_seqs, max_pages;
@@ -399,7 +399,13 @@ spear_status spear_kv_reserve(const spear_kv_pool* pool, const int32_t* rows, co
  */
 spear_status spear_kv_fork(const spear_kv_pool* pool, const spear_kv_cache* caches, int ncaches,
                            const int32_t* parents, const int32_t* children, int n, void* stream);
-/* Empties the sequences: every page's count goes down, rows become -1, lengths 0.  An empty one stays as it is. */
+/*
+ * Empties the sequences: every page's count goes down, rows become -1, lengths
+ * 0.  Each by itself: one that is listed twice is emptied once, an empty one
+ * stays as it is, and one that is out of range, or whose length is, is
+ * reported and left as it is while the others are emptied.  A page number out
+ * of range, or a page whose count is 0 already, is reported.
+ */
 spear_status spear_kv_free(const spear_kv_pool* pool, const int32_t* rows, int n, void* stream);
 /*
  * Moves the live pages to the front of the pool: with L of them, the i-th one

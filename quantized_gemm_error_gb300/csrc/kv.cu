@@ -277,7 +277,8 @@ pool_take_kernel(PoolView p, const int32_t* rows, const int32_t* arg, int n) {
 }
 
 // One block a freed row; the exchange of the length makes a row that is
-// listed twice (or is empty already) a no-op.
+// listed twice (or is empty already) a no-op.  A row whose length is out of
+// range stays as it is: what it holds is not known.
 __global__ void __launch_bounds__(256) pool_free_kernel(PoolView p, const int32_t* rows) {
   __shared__ int s_len;
   enter();
@@ -286,20 +287,25 @@ __global__ void __launch_bounds__(256) pool_free_kernel(PoolView p, const int32_
     if (threadIdx.x == 0) record_status(&g_kv_status, DEV_ERR_INVALID);
     return;
   }
-  if (threadIdx.x == 0) s_len = atomicExch(&p.lens[row], 0);
+  if (threadIdx.x == 0) {
+    const int at = p.lens[row];
+    const bool bad = at < 0 || (long long)at > (long long)p.max_pages * p.page.d;
+    if (bad) record_status(&g_kv_status, DEV_ERR_INVALID);
+    s_len = bad ? 0 : atomicExch(&p.lens[row], 0);
+  }
   __syncthreads();
   const int len = s_len;
-  if (len < 0 || (long long)len > (long long)p.max_pages * p.page.d) {
-    if (threadIdx.x == 0) record_status(&g_kv_status, DEV_ERR_INVALID);
-    return;
-  }
   const int held = (int)p.page.div((uint32_t)len + p.page.d - 1);
   for (int j = threadIdx.x; j < held; j += 256) {
     int32_t* e = p.table + (int64_t)row * p.max_pages + j;
     const int pg = *e;
     *e = -1;
-    if ((unsigned)pg >= (unsigned)p.num_pages || atomicSub(&p.refs[pg], 1) <= 0)
+    if ((unsigned)pg >= (unsigned)p.num_pages) {
       record_status(&g_kv_status, DEV_ERR_INVALID);
+    } else if (atomicSub(&p.refs[pg], 1) <= 0) {    // nobody's page: it stays free
+      atomicAdd(&p.refs[pg], 1);
+      record_status(&g_kv_status, DEV_ERR_INVALID);
+    }
   }
 }
 
