@@ -420,7 +420,7 @@ class KVCache:
             raise ValueError("a cache row's elements must be contiguous")
         if not k.is_cuda or k.device != v.device:
             raise ValueError("k and v must be on one CUDA device")
-        self.k, self.v = k, v
+        self.k, self.v, self.index = k, v, k.get_device()
         self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = k.shape
         self.dtype, self.device = k.dtype, k.device
         self.c = _Cache(self.num_pages, self.page_size, self.num_kv_heads, self.head_dim, _DT_OF[k.dtype],
@@ -457,7 +457,7 @@ class PagePool:
         # page moves of the last fork or compact: [0] their number, pairs (source, destination) from [2]; [1] is odd
         # while the last reserve was refused
         self.moves = torch.zeros(2 + 3 * num_pages, dtype=torch.int32, device=device)
-        self.device = self.state.device
+        self.device, self.index = self.state.device, self.state.get_device()
         self.c = _Pool(num_pages, page_size, max_seqs, max_pages, self.refs.data_ptr(), self.seq_lens.data_ptr(),
                        self.block_table.data_ptr(), self.moves.data_ptr())
         self.ref = ctypes.byref(self.c)
@@ -471,13 +471,26 @@ class PagePool:
         self.state.copy_(saved)
 
 
-def _bytes_ptr(t: torch.Tensor) -> int:
-    if t.dtype is not torch.uint8 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 CUDA tensor, got {t.dtype} on {t.device}")
+# The tensors of a call are on the device of its cache or pool (`dev`, an index), which is the current one: the library
+# launches there.
+
+def _stream_on(dev: int, stream) -> int:
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"the call's tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is not None and getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"the call's tensors are on cuda:{dev}, its stream on cuda:{stream.device_index}")
+    return _raw_stream(stream)
+
+
+def _bytes_ptr(t: torch.Tensor, dev: int) -> int:
+    if t.dtype is not torch.uint8 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{dev}, got {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
-def _i32(t: torch.Tensor, name: str, n: Optional[int] = None) -> int:
+def _i32(t: torch.Tensor, name: str, n: Optional[int] = None, dev: Optional[int] = None) -> int:
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_cuda or (n is not None and t.shape[0] != n):
         raise ValueError(f"{name} must be a 1-D int32 CUDA tensor{'' if n is None else f' of {n}'}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
@@ -486,43 +499,43 @@ def _i32(t: torch.Tensor, name: str, n: Optional[int] = None) -> int:
     return t.data_ptr()
 
 
-def _seqs(table: torch.Tensor, lens: torch.Tensor, ids: Optional[torch.Tensor], n: int) -> _Seqs:
-    if table.dtype is not torch.int32 or table.dim() != 2 or not table.is_cuda or table.stride(1) != 1:
-        raise ValueError("block_table must be an int32 CUDA [rows][max_pages] tensor with contiguous rows")
+def _seqs(table: torch.Tensor, lens: torch.Tensor, ids: Optional[torch.Tensor], n: int, dev: int) -> _Seqs:
+    if table.dtype is not torch.int32 or table.dim() != 2 or table.get_device() != dev or table.stride(1) != 1:
+        raise ValueError(f"block_table must be an int32 [rows][max_pages] tensor on cuda:{dev} with contiguous rows")
     rows, cols = table.shape
     if ids is None and n > rows:
         raise ValueError(f"{n} sequences, but block_table has {rows} rows")
-    return _Seqs(n, cols, rows, table.stride(0) if rows > 1 else cols, table.data_ptr(), _i32(lens, "seq_lens", rows),
-                 None if ids is None else _i32(ids, "seq_ids", n))
+    return _Seqs(n, cols, rows, table.stride(0) if rows > 1 else cols, table.data_ptr(), _i32(lens, "seq_lens", rows, dev),
+                 None if ids is None else _i32(ids, "seq_ids", n, dev))
 
 
-def _token_rows(t: torch.Tensor, name: str, dtype, heads: Optional[int], D: int):
+def _token_rows(t: torch.Tensor, name: str, dtype, heads: Optional[int], D: int, dev: int):
     """(tokens, heads, token stride, head stride) of q or of new K/V rows; the stride of an extent of one counts as 0."""
     if t.dim() != 3 or t.dtype is not dtype or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be {dtype} [tokens][{'heads' if heads is None else heads}][{D}], got {t.dtype} "
                          f"{tuple(t.shape)}")
     st, sh, sd = t.stride()
-    if sd != 1 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor whose rows of {D} elements are contiguous")
+    if sd != 1 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev} whose rows of {D} elements are contiguous, got {t.device}")
     T, H, _ = t.shape
     return T, H, st if T > 1 else 0, sh if H > 1 else 0
 
 
 def _attn(q, cache, scale, window, sinks, out, lse, stream):
-    D = cache.head_dim
-    T, H, st, sh = _token_rows(q, "q", cache.dtype, None, D)
+    D, dev = cache.head_dim, cache.index
+    T, H, st, sh = _token_rows(q, "q", cache.dtype, None, D, dev)
     if out is None:
         out = _made_on(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
-    elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous() or not out.is_cuda:
-        raise ValueError(f"out must be a contiguous {q.dtype} {tuple(q.shape)} CUDA tensor, got {out.dtype} "
-                         f"{tuple(out.shape)}")
+    elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError(f"out must be a contiguous {q.dtype} {tuple(q.shape)} tensor on cuda:{dev}, got {out.dtype} "
+                         f"{tuple(out.shape)} on {out.device}")
     if lse is None:
         p_lse = None
-    elif lse.dtype is torch.float32 and lse.shape == (T, H) and lse.is_contiguous() and lse.is_cuda:
+    elif lse.dtype is torch.float32 and lse.shape == (T, H) and lse.is_contiguous() and lse.get_device() == dev:
         p_lse = lse.data_ptr()
     else:
-        raise ValueError(f"lse must be a contiguous float32 [{T}][{H}] CUDA tensor, got {lse.dtype} "
-                         f"{tuple(lse.shape)}")
+        raise ValueError(f"lse must be a contiguous float32 [{T}][{H}] tensor on cuda:{dev}, got {lse.dtype} "
+                         f"{tuple(lse.shape)} on {lse.device}")
     return out, _Attn(q.data_ptr(), st, sh, H, D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
                       p_lse)
 
@@ -534,16 +547,19 @@ def spear_kv_append(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, bl
     starts[b + 1]) are the last tokens of sequence b, whose length seq_lens counts them already.  Pass the `pool`
     whose spear_kv_reserve made room for them: where it was refused the call then writes nothing and reports
     SPEAR_ERR_INVALID_ARG (without it the rows would replace the sequences' last cached ones)."""
-    T, _, kt, kh = _token_rows(k_new, "k_new", cache.dtype, cache.num_kv_heads, cache.head_dim)
-    Tv, _, vt, vh = _token_rows(v_new, "v_new", cache.dtype, cache.num_kv_heads, cache.head_dim)
+    dev = cache.index
+    T, _, kt, kh = _token_rows(k_new, "k_new", cache.dtype, cache.num_kv_heads, cache.head_dim, dev)
+    Tv, _, vt, vh = _token_rows(v_new, "v_new", cache.dtype, cache.num_kv_heads, cache.head_dim, dev)
     if T != Tv:
         raise ValueError(f"k_new has {T} tokens, v_new {Tv}")
-    p_starts, n = _i32(starts, "starts"), starts.shape[0] - 1
-    s = _seqs(block_table, seq_lens, seq_ids, n)
+    p_starts, n = _i32(starts, "starts", None, dev), starts.shape[0] - 1
+    s = _seqs(block_table, seq_lens, seq_ids, n, dev)
     if pool is not None:
+        if pool.index != dev:
+            raise ValueError(f"pool must be on cuda:{dev}, got {pool.device}")
         s.refused = pool.c.moves + 4
     _check(load().spear_kv_append(cache.ref, ctypes.byref(s), p_starts, T, k_new.data_ptr(), kt, kh,
-                                  v_new.data_ptr(), vt, vh, _raw_stream(stream)), "spear_kv_append")
+                                  v_new.data_ptr(), vt, vh, _stream_on(dev, stream)), "spear_kv_append")
 
 
 def spear_attn_decode_workspace_bytes(cache: KVCache, num_seqs: int, num_q_heads: int) -> int:
@@ -559,13 +575,14 @@ def spear_attn_decode(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor
                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of one new token of each sequence, q [seqs][q_heads][head_dim], over its cached keys (its own among
     them); scale defaults to head_dim ** -0.5.  `lse`, when given, receives the rows' log sums (fp32)."""
+    raw, dev = _stream_on(cache.index, stream), cache.index
     out, a = _attn(q, cache, scale, window, sinks, out, lse, stream)
-    s = _seqs(block_table, seq_lens, seq_ids, q.shape[0])
+    s = _seqs(block_table, seq_lens, seq_ids, q.shape[0], dev)
     if workspace is None:
         workspace = cache._workspace("attn_decode", (s.num_seqs, a.num_q_heads), spear_attn_decode_workspace_bytes, True,
                                      stream)
-    _check(load().spear_attn_decode(cache.ref, ctypes.byref(s), ctypes.byref(a), _bytes_ptr(workspace),
-                                    workspace.numel(), _raw_stream(stream)), "spear_attn_decode")
+    _check(load().spear_attn_decode(cache.ref, ctypes.byref(s), ctypes.byref(a), _bytes_ptr(workspace, dev),
+                                    workspace.numel(), raw), "spear_attn_decode")
     return out
 
 
@@ -583,27 +600,31 @@ def spear_attn_prefill(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Causal attention of a ragged batch of new tokens, q [tokens][q_heads][head_dim], rows [starts[b],
     starts[b + 1]) the last tokens of sequence b; their K and V rows are in the cache already."""
+    raw, dev = _stream_on(cache.index, stream), cache.index
     out, a = _attn(q, cache, scale, window, sinks, out, lse, stream)
-    p_starts, n = _i32(starts, "starts"), starts.shape[0] - 1
-    s = _seqs(block_table, seq_lens, seq_ids, n)
+    p_starts, n = _i32(starts, "starts", None, dev), starts.shape[0] - 1
+    s = _seqs(block_table, seq_lens, seq_ids, n, dev)
     T = out.shape[0]
     if workspace is None:
         workspace = cache._workspace("attn_prefill", (n, T, a.num_q_heads), spear_attn_prefill_workspace_bytes, False,
                                      stream)
-    _check(load().spear_attn_prefill(cache.ref, ctypes.byref(s), p_starts, T, ctypes.byref(a), _bytes_ptr(workspace),
-                                     workspace.numel(), _raw_stream(stream)), "spear_attn_prefill")
+    _check(load().spear_attn_prefill(cache.ref, ctypes.byref(s), p_starts, T, ctypes.byref(a), _bytes_ptr(workspace, dev),
+                                     workspace.numel(), raw), "spear_attn_prefill")
     return out
 
 
 def spear_kv_reserve(pool: PagePool, rows: torch.Tensor, tokens: torch.Tensor, *, stream=None) -> None:
     """Lengthens each listed sequence by tokens[i], taking the pages it needs (the lowest free ones, in order)."""
-    p_rows, n = _i32(rows, "rows"), rows.shape[0]
-    _check(load().spear_kv_reserve(pool.ref, p_rows, _i32(tokens, "tokens", n), n, _raw_stream(stream)),
+    p_rows, n, dev = _i32(rows, "rows", None, pool.index), rows.shape[0], pool.index
+    _check(load().spear_kv_reserve(pool.ref, p_rows, _i32(tokens, "tokens", n, dev), n, _stream_on(dev, stream)),
            "spear_kv_reserve")
 
 
-def _caches(caches):
+def _caches(caches, dev: int):
     """(C array, count) of one cache or a list of them."""
+    for c in (caches,) if isinstance(caches, KVCache) else caches:
+        if c.index != dev:
+            raise ValueError(f"the caches must be on cuda:{dev}, got {c.device}")
     if isinstance(caches, KVCache):
         return caches.ref, 1
     return (_Cache * max(1, len(caches)))(*[c.c for c in caches]), len(caches)
@@ -612,21 +633,22 @@ def _caches(caches):
 def spear_kv_fork(pool: PagePool, caches, parents: torch.Tensor, children: torch.Tensor, *, stream=None) -> None:
     """Makes each empty sequence children[i] a copy of parents[i]: whole pages shared, a partly filled one copied in
     every cache (one KVCache, or the list of all layers')."""
-    p_par, n = _i32(parents, "parents"), parents.shape[0]
-    arr, count = _caches(caches)
-    _check(load().spear_kv_fork(pool.ref, arr, count, p_par, _i32(children, "children", n), n, _raw_stream(stream)),
-           "spear_kv_fork")
+    p_par, n, dev = _i32(parents, "parents", None, pool.index), parents.shape[0], pool.index
+    arr, count = _caches(caches, dev)
+    _check(load().spear_kv_fork(pool.ref, arr, count, p_par, _i32(children, "children", n, dev), n,
+                                _stream_on(dev, stream)), "spear_kv_fork")
 
 
 def spear_kv_free(pool: PagePool, rows: torch.Tensor, *, stream=None) -> None:
     """Empties the listed sequences and gives up their references to pages."""
-    _check(load().spear_kv_free(pool.ref, _i32(rows, "rows"), rows.shape[0], _raw_stream(stream)), "spear_kv_free")
+    _check(load().spear_kv_free(pool.ref, _i32(rows, "rows", None, pool.index), rows.shape[0],
+                                _stream_on(pool.index, stream)), "spear_kv_free")
 
 
 def spear_kv_compact(pool: PagePool, caches, *, stream=None) -> None:
     """Moves the live pages of every cache to the front of the pool and renames them in the block table."""
-    arr, count = _caches(caches)
-    _check(load().spear_kv_compact(pool.ref, arr, count, _raw_stream(stream)), "spear_kv_compact")
+    arr, count = _caches(caches, pool.index)
+    _check(load().spear_kv_compact(pool.ref, arr, count, _stream_on(pool.index, stream)), "spear_kv_compact")
 
 
 def spear_kv_copy_pages(caches, moves: torch.Tensor, max_moves: Optional[int] = None, *, stream=None) -> None:
@@ -634,9 +656,10 @@ def spear_kv_copy_pages(caches, moves: torch.Tensor, max_moves: Optional[int] = 
     p_moves, room = _i32(moves, "moves"), (moves.shape[0] - 2) // 2
     if room < 0 or (max_moves is not None and max_moves > room):
         raise ValueError(f"moves holds {moves.shape[0]} words: 2, and 2 for each of up to {max_moves} pairs")
-    arr, count = _caches(caches)
+    dev = moves.get_device()
+    arr, count = _caches(caches, dev)
     _check(load().spear_kv_copy_pages(arr, count, p_moves, room if max_moves is None else max_moves,
-                                      _raw_stream(stream)), "spear_kv_copy_pages")
+                                      _stream_on(dev, stream)), "spear_kv_copy_pages")
 
 
 # ------------------------------------------------------- module selection
