@@ -402,6 +402,7 @@ def spear_linear_prefill(layer: W4Layer, x: torch.Tensor, *, y=None, out_dtype: 
 
 # ------------------------------------- paged key/value cache and attention
 
+_INT_MIN, _INT_MAX = -0x80000000, 0x7fffffff
 _DT_OF = {torch.bfloat16: DT_BF16, torch.float16: DT_F16}
 
 
@@ -522,6 +523,8 @@ def _token_rows(t: torch.Tensor, name: str, dtype, heads: Optional[int], D: int,
 
 
 def _attn(q, cache, scale, window, sinks, out, lse, stream):
+    if not (_INT_MIN <= window <= _INT_MAX and _INT_MIN <= sinks <= _INT_MAX):         # ctypes would cut them to 32 bits
+        raise ValueError(f"window and sinks are 32-bit numbers, got {window} and {sinks}")
     D, dev = cache.head_dim, cache.index
     T, H, st, sh = _token_rows(q, "q", cache.dtype, None, D, dev)
     if out is None:
