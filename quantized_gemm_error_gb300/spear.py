@@ -427,13 +427,13 @@ class KVCache:
         self.c = _Cache(self.num_pages, self.page_size, self.num_kv_heads, self.head_dim, _DT_OF[k.dtype],
                         k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2))
         self.ref = ctypes.byref(self.c)
-        self._ws_bytes = {}                           # workspace bytes by call and sizes
+        self._ws_bytes = {}                           # workspace bytes by call: the head size and the device make them
 
     def _workspace(self, kind: str, sizes: tuple, fn, zero: bool, stream) -> torch.Tensor:
         """The binding's workspace for a call on this cache (see _default_workspace)."""
-        n = self._ws_bytes.get((kind, sizes))
+        n = self._ws_bytes.get(kind)
         if n is None:
-            n = self._ws_bytes[kind, sizes] = fn(self, *sizes)
+            n = self._ws_bytes[kind] = fn(self, *sizes)
         return _default_workspace(kind, n, self.device, stream, zero)
 
 
