@@ -129,6 +129,19 @@ int check_pool_caches(const spear_kv_pool& p, const spear_kv_cache* c, int n) {
                 c[0].page_size, p.num_pages, p.page_size);
   return SPEAR_OK;
 }
+
+// The kernels' status words, in the order in which the first one set is
+// reported.  One kernel takes and clears them all and one copy brings them
+// over: 9 copies and clears one after another took 110 us a call.
+constexpr int kStatusWords = 9;
+int (*const kStatusWordOf[kStatusWords])(unsigned**) = {
+    status_word_pack,    status_word_decode,  status_word_decode_tm, status_word_decode_ks,    status_word_decode_tc,
+    status_word_prefill, status_word_kv,      status_word_attn_decode, status_word_attn_prefill};
+struct StatusWords {
+  unsigned* w[kStatusWords];
+};
+__device__ unsigned g_taken[kStatusWords];
+__global__ void take_status_kernel(StatusWords s) { g_taken[threadIdx.x] = atomicExch(s.w[threadIdx.x], 0u); }
 }  // namespace
 
 void set_last_error(const char* msg) { snprintf(t_last_error, sizeof(t_last_error), "%s", msg ? msg : ""); }
@@ -517,22 +530,22 @@ spear_status spear_set_launch_overlap(int enable) {
 spear_status spear_get_device_status(int* out, void* stream) {
   if (!out) return fail(SPEAR_ERR_INVALID_ARG, "out is NULL");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  unsigned s_pack = 0, s_dec = 0, s_pre = 0;
-  if (int rc = read_and_clear_status_pack(&s_pack, st)) return rc;
-  unsigned s_dtc = 0, s_dks = 0, s_dtm = 0;
-  if (int rc = read_and_clear_status_decode(&s_dec, st)) return rc;
-  if (int rc = read_and_clear_status_decode_tc(&s_dtc, st)) return rc;
-  if (int rc = read_and_clear_status_decode_ks(&s_dks, st)) return rc;
-  if (int rc = read_and_clear_status_decode_tm(&s_dtm, st)) return rc;
-  if (!s_dec) s_dec = s_dtm ? s_dtm : s_dks ? s_dks : s_dtc;
-  if (int rc = read_and_clear_status_prefill(&s_pre, st)) return rc;
-  unsigned s_kv = 0, s_ad = 0, s_ap = 0;
-  if (int rc = read_and_clear_status_kv(&s_kv, st)) return rc;
-  if (int rc = read_and_clear_status_attn_decode(&s_ad, st)) return rc;
-  if (int rc = read_and_clear_status_attn_prefill(&s_ap, st)) return rc;
-  if (!s_pre) s_pre = s_kv ? s_kv : s_ad ? s_ad : s_ap;
-  if (int rc = cuda_check(cudaStreamSynchronize(st), "status sync")) return rc;
-  *out = (int)(s_pack ? s_pack : s_dec ? s_dec : s_pre);
+  StatusWords words;
+  for (int i = 0; i < kStatusWords; ++i)
+    if (int rc = kStatusWordOf[i](&words.w[i])) return rc;
+  unsigned seen[kStatusWords] = {};
+  {
+    static std::mutex mu;                            // g_taken is everyone's
+    std::lock_guard<std::mutex> lk(mu);
+    take_status_kernel<<<1, kStatusWords, 0, st>>>(words);
+    if (int rc = cuda_check(cudaGetLastError(), "status launch")) return rc;
+    if (int rc = cuda_check(cudaMemcpyFromSymbolAsync(seen, g_taken, sizeof(seen), 0, cudaMemcpyDeviceToHost, st),
+                            "read status")) return rc;
+    if (int rc = cuda_check(cudaStreamSynchronize(st), "status sync")) return rc;
+  }
+  *out = SPEAR_OK;
+  for (int i = kStatusWords - 1; i >= 0; --i)
+    if (seen[i]) *out = (int)seen[i];
   return SPEAR_OK;
 }
 

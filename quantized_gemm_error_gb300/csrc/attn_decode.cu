@@ -642,12 +642,8 @@ int launch_attn_decode(const spear_kv_cache& c, const spear_kv_seqs& s, const sp
   return f16 ? launch<128, true, 1>(a, blocks, st) : launch<128, false, 1>(a, blocks, st);
 }
 
-int read_and_clear_status_attn_decode(unsigned* out, cudaStream_t st) {
-  void* addr = nullptr;
-  if (int rc = cuda_check(cudaGetSymbolAddress(&addr, g_attn_decode_status), "attn_decode status address")) return rc;
-  if (int rc = cuda_check(cudaMemcpyAsync(out, addr, sizeof(unsigned), cudaMemcpyDeviceToHost, st), "read attn_decode status")) return rc;
-  if (int rc = cuda_check(cudaStreamSynchronize(st), "read attn_decode status")) return rc;
-  return cuda_check(cudaMemsetAsync(addr, 0, sizeof(unsigned), st), "clear attn_decode status");
+int status_word_attn_decode(unsigned** word) {
+  return cuda_check(cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_attn_decode_status), "attn_decode status address");
 }
 
 }  // namespace spear

@@ -1376,12 +1376,8 @@ int launch_attn_prefill(const spear_kv_cache& c, const spear_kv_seqs& s, const i
   return f16 ? launch<128, true>(a, maps, di.num_sms, st) : launch<128, false>(a, maps, di.num_sms, st);
 }
 
-int read_and_clear_status_attn_prefill(unsigned* out, cudaStream_t st) {
-  void* addr = nullptr;
-  if (int rc = cuda_check(cudaGetSymbolAddress(&addr, g_attn_prefill_status), "attn_prefill status address")) return rc;
-  if (int rc = cuda_check(cudaMemcpyAsync(out, addr, sizeof(unsigned), cudaMemcpyDeviceToHost, st), "read attn_prefill status")) return rc;
-  if (int rc = cuda_check(cudaStreamSynchronize(st), "read attn_prefill status")) return rc;
-  return cuda_check(cudaMemsetAsync(addr, 0, sizeof(unsigned), st), "clear attn_prefill status");
+int status_word_attn_prefill(unsigned** word) {
+  return cuda_check(cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_attn_prefill_status), "attn_prefill status address");
 }
 
 }  // namespace spear

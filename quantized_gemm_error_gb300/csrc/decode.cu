@@ -1005,12 +1005,8 @@ int launch_decode_noalloc(const spear_w4_layer& L, const uint16_t* x, int M, voi
   return launch_decode(L, x, M, y, out_f32, ws, kNoallocScratchBytes, st, false);
 }
 
-int read_and_clear_status_decode(unsigned* out, cudaStream_t st) {
-  void* addr = nullptr;
-  if (int rc = cuda_check(cudaGetSymbolAddress(&addr, g_decode_status), "decode status address")) return rc;
-  if (int rc = cuda_check(cudaMemcpyAsync(out, addr, sizeof(unsigned), cudaMemcpyDeviceToHost, st), "read decode status")) return rc;
-  if (int rc = cuda_check(cudaStreamSynchronize(st), "read decode status")) return rc;
-  return cuda_check(cudaMemsetAsync(addr, 0, sizeof(unsigned), st), "clear decode status");
+int status_word_decode(unsigned** word) {
+  return cuda_check(cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_decode_status), "decode status address");
 }
 
 }  // namespace spear

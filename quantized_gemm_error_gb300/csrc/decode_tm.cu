@@ -1103,13 +1103,8 @@ int launch_decode_tm(const spear_w4_layer& L, const uint16_t* x, int M, void* y,
   return cuda_check(cudaLaunchKernelEx(&cfg, pl.fn, tm_w, tm_x, tm_a, p), "decode launch");
 }
 
-int read_and_clear_status_decode_tm(unsigned* out, cudaStream_t st) {
-  void* addr = nullptr;
-  if (int rc = cuda_check(cudaGetSymbolAddress(&addr, g_dtm_status), "decode status address")) return rc;
-  if (int rc = cuda_check(cudaMemcpyAsync(out, addr, sizeof(unsigned), cudaMemcpyDeviceToHost, st),
-                          "read decode status")) return rc;
-  if (int rc = cuda_check(cudaStreamSynchronize(st), "read decode status")) return rc;
-  return cuda_check(cudaMemsetAsync(addr, 0, sizeof(unsigned), st), "clear decode status");
+int status_word_decode_tm(unsigned** word) {
+  return cuda_check(cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_dtm_status), "decode status address");
 }
 
 }  // namespace spear

@@ -47,7 +47,7 @@ int ensure_smem_limit(const void* fn, size_t bytes);
 // ---- pack.cu
 int launch_pack_w4(const float* W, int N, int K, int G, int sym, uint8_t* qweight,
                    uint16_t* scales, uint8_t* zeros, cudaStream_t st);
-int read_and_clear_status_pack(unsigned* out, cudaStream_t st);
+int status_word_pack(unsigned** word);
 
 // ---- decode.cu
 int decode_workspace_bytes(const spear_w4_layer& L, int M, size_t* bytes);
@@ -55,32 +55,32 @@ int launch_decode(const spear_w4_layer& L, const uint16_t* x, int M, void* y, in
                   void* ws, size_t ws_bytes, cudaStream_t st, bool overlap);
 int launch_decode_noalloc(const spear_w4_layer& L, const uint16_t* x, int M, void* y, int out_f32,
                           cudaStream_t st);
-int read_and_clear_status_decode(unsigned* out, cudaStream_t st);
+int status_word_decode(unsigned** word);
 
 // ---- decode_ks.cu (cluster K-split decode, 1..32 tokens, no workspace)
 bool decode_ks_supports(const spear_w4_layer& L, int M);
 int launch_decode_ks(const spear_w4_layer& L, const uint16_t* x, int M, void* y, int out_f32, cudaStream_t st,
                      bool overlap);
-int read_and_clear_status_decode_ks(unsigned* out, cudaStream_t st);
+int status_word_decode_ks(unsigned** word);
 
 // ---- decode_tm.cu (cluster K-split decode on tcgen05, weights in tensor memory, 1..64 tokens)
 bool decode_tm_supports(const spear_w4_layer& L, int M);
 int launch_decode_tm(const spear_w4_layer& L, const uint16_t* x, int M, void* y, int out_f32, cudaStream_t st,
                      bool overlap);
-int read_and_clear_status_decode_tm(unsigned* out, cudaStream_t st);
+int status_word_decode_tm(unsigned** word);
 
 // ---- decode_tc.cu (tensor-core decode path)
 int decode_tc_workspace_bytes(const spear_w4_layer& L, int M, size_t* bytes);
 size_t decode_tc_sync_bytes();
 int launch_decode_tc(const spear_w4_layer& L, const uint16_t* x, int M, void* y, int out_f32, void* ws,
                      size_t ws_bytes, cudaStream_t st, bool overlap);
-int read_and_clear_status_decode_tc(unsigned* out, cudaStream_t st);
+int status_word_decode_tc(unsigned** word);
 
 // ---- prefill.cu
 int prefill_workspace_bytes(const spear_w4_layer& L, int M, int mode, size_t* bytes);
 int launch_prefill(const spear_w4_layer& L, const uint16_t* x, int M, void* y, int out_f32,
                    int mode, void* ws, size_t ws_bytes, cudaStream_t st, cudaStream_t st_aux);
-int read_and_clear_status_prefill(unsigned* out, cudaStream_t st);
+int status_word_prefill(unsigned** word);
 
 // ---- kv.cu (the paged key/value cache)
 int launch_kv_append(const spear_kv_cache& c, const spear_kv_seqs& s, const int32_t* starts, int tokens,
@@ -93,16 +93,16 @@ int launch_kv_free(const spear_kv_pool& p, const int32_t* rows, int n, cudaStrea
 int launch_kv_fork(const spear_kv_pool& p, const spear_kv_cache* caches, int ncaches, const int32_t* parents,
                    const int32_t* children, int n, cudaStream_t st);
 int launch_kv_compact(const spear_kv_pool& p, const spear_kv_cache* caches, int ncaches, cudaStream_t st);
-int read_and_clear_status_kv(unsigned* out, cudaStream_t st);
+int status_word_kv(unsigned** word);
 
 // ---- attn_decode.cu, attn_prefill.cu (attention over the cache)
 int attn_decode_workspace_bytes(const spear_kv_cache& c, int nseqs, int q_heads, size_t* bytes);
 int launch_attn_decode(const spear_kv_cache& c, const spear_kv_seqs& s, const spear_attn& a, void* ws,
                        size_t ws_bytes, cudaStream_t st);
-int read_and_clear_status_attn_decode(unsigned* out, cudaStream_t st);
+int status_word_attn_decode(unsigned** word);
 int attn_prefill_workspace_bytes(const spear_kv_cache& c, int nseqs, int tokens, int q_heads, size_t* bytes);
 int launch_attn_prefill(const spear_kv_cache& c, const spear_kv_seqs& s, const int32_t* starts, int tokens,
                         const spear_attn& a, void* ws, size_t ws_bytes, cudaStream_t st);
-int read_and_clear_status_attn_prefill(unsigned* out, cudaStream_t st);
+int status_word_attn_prefill(unsigned** word);
 
 }  // namespace spear

@@ -545,12 +545,8 @@ int launch_kv_compact(const spear_kv_pool& p, const spear_kv_cache* caches, int 
   return ncaches > first ? launch_kv_copy_pages(caches + first, ncaches - first, p.moves, p.num_pages, st) : SPEAR_OK;
 }
 
-int read_and_clear_status_kv(unsigned* out, cudaStream_t st) {
-  void* addr = nullptr;
-  if (int rc = cuda_check(cudaGetSymbolAddress(&addr, g_kv_status), "kv status address")) return rc;
-  if (int rc = cuda_check(cudaMemcpyAsync(out, addr, sizeof(unsigned), cudaMemcpyDeviceToHost, st), "read kv status")) return rc;
-  if (int rc = cuda_check(cudaStreamSynchronize(st), "read kv status")) return rc;
-  return cuda_check(cudaMemsetAsync(addr, 0, sizeof(unsigned), st), "clear kv status");
+int status_word_kv(unsigned** word) {
+  return cuda_check(cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_kv_status), "kv status address");
 }
 
 }  // namespace spear

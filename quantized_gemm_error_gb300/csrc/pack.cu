@@ -128,12 +128,8 @@ int launch_pack_w4(const float* W, int N, int K, int G, int sym, uint8_t* qweigh
   return cuda_check(cudaGetLastError(), "pack_w4 launch");
 }
 
-int read_and_clear_status_pack(unsigned* out, cudaStream_t st) {
-  void* addr = nullptr;
-  if (int rc = cuda_check(cudaGetSymbolAddress(&addr, g_pack_status), "pack status address")) return rc;
-  if (int rc = cuda_check(cudaMemcpyAsync(out, addr, sizeof(unsigned), cudaMemcpyDeviceToHost, st), "read pack status")) return rc;
-  if (int rc = cuda_check(cudaStreamSynchronize(st), "read pack status")) return rc;
-  return cuda_check(cudaMemsetAsync(addr, 0, sizeof(unsigned), st), "clear pack status");
+int status_word_pack(unsigned** word) {
+  return cuda_check(cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_pack_status), "pack status address");
 }
 
 }  // namespace spear

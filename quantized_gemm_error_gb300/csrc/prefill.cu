@@ -1035,12 +1035,8 @@ int launch_prefill(const spear_w4_layer& L, const uint16_t* x, int M, void* y, i
   return launch_comp_up(L, M, y, out_f32, y32, T2, st);
 }
 
-int read_and_clear_status_prefill(unsigned* out, cudaStream_t st) {
-  void* addr = nullptr;
-  if (int rc = cuda_check(cudaGetSymbolAddress(&addr, g_prefill_status), "prefill status address")) return rc;
-  if (int rc = cuda_check(cudaMemcpyAsync(out, addr, sizeof(unsigned), cudaMemcpyDeviceToHost, st), "read prefill status")) return rc;
-  if (int rc = cuda_check(cudaStreamSynchronize(st), "read prefill status")) return rc;
-  return cuda_check(cudaMemsetAsync(addr, 0, sizeof(unsigned), st), "clear prefill status");
+int status_word_prefill(unsigned** word) {
+  return cuda_check(cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_prefill_status), "prefill status address");
 }
 
 }  // namespace spear
