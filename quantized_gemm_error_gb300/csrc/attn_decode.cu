@@ -39,7 +39,6 @@ constexpr int kUnit = 16;                           // keys of a unit
 constexpr int kGroups = 2048;                       // entries of the prefix over sequences
 constexpr int kKept = 1024;                         // sequences whose rows and lengths are kept in shared memory
 constexpr int kRingBytes = 192 * 1024;
-constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 constexpr int kMaxHeads = 16;                       // query heads of an item
 // P is taken times 2^kLift: in fp16 a probability is normal down to 2^-28 of
 // its row's largest so (19 nats; unlifted 2^-14, and below 2^-25 it would be 0,
@@ -67,9 +66,6 @@ struct DecArgs {
 
 __host__ __device__ constexpr int part_floats(int D) { return kMaxHeads * (D + 2); }
 
-__device__ __forceinline__ void cp_async16_zfill(uint32_t s, const void* g, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(g), "r"(valid ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -83,11 +79,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 template <bool F16>
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -127,11 +118,6 @@ struct Cursor {
   }
 };
 
-// p / z for 0 <= p < 2^63 and z > 0; in 32 bits where both fit.
-__device__ __forceinline__ long long divide(long long p, long long z) {
-  if ((((unsigned long long)p | (unsigned long long)z) >> 32) == 0) return (uint32_t)p / (uint32_t)z;
-  return (long long)((unsigned long long)p / (unsigned long long)z);
-}
 // Inclusive prefix sum over the warp.
 __device__ __forceinline__ long long warp_scan(long long v, int lane) {
 #pragma unroll

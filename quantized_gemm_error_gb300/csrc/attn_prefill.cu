@@ -60,7 +60,6 @@ constexpr int kThreads = 512;
 constexpr int kMmaWarp = 8, kTmaWarp = 9, kQWarp = 10, kMmaWarp1 = 11, kLoadWarp = 12, kLoadThreads = 128;
 constexpr int kGroups = 2048;                       // entries of the prefix over sequences
 constexpr int kKept = 4096;                         // sequences whose lengths are kept in shared memory meanwhile
-constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 constexpr uint64_t kLandNs = 2000000000ull;         // limit of the waits for a block's own copies and MMAs, which end by themselves
 // log2 growth of a row maximum that is let pass: P's largest values are then up
 // to 2^15 apart.  With 8 a row that sees four sinks first is rescaled once more: windowed
@@ -134,15 +133,6 @@ struct Layout {
   static constexpr int kQ = 0, kRing = 2 * kTileBytes, kTotal = kRing + kSlots * kTileBytes;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ void cp_async16_zfill(uint32_t s, const void* g, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(g), "r"(valid ? 16 : 0) : "memory");
-}
-
 template <int S, int G>                              // constant offsets of both addresses
 __device__ __forceinline__ void cp_async16(uint32_t s, uint64_t g) {
   asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(s), "l"(g), "n"(S), "n"(G) : "memory");
@@ -212,12 +202,6 @@ __device__ __forceinline__ long long seq_units(const PreArgs& a, const Seq& s) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
   return sum;
-}
-
-// p / z for 0 <= p < 2^63 and z > 0; in 32 bits where both fit.
-__device__ __forceinline__ long long divide(long long p, long long z) {
-  if ((((unsigned long long)p | (unsigned long long)z) >> 32) == 0) return (uint32_t)p / (uint32_t)z;
-  return (long long)((unsigned long long)p / (unsigned long long)z);
 }
 
 // Where a block's units start, and its pieces: consecutive tiles of an item.

@@ -126,10 +126,6 @@ template <bool F16>
 __device__ __forceinline__ float elem_to_f32(uint16_t b) {
   return F16 ? f16_bits_to_f32(b) : __uint_as_float((uint32_t)b << 16);
 }
-template <bool F16>
-__device__ __forceinline__ uint16_t f32_to_elem(float f) {
-  return F16 ? __half_as_ushort(__float2half_rn(f)) : __bfloat16_as_ushort(__float2bfloat16_rn(f));
-}
 // Two floats rounded to nearest even, `lo` in the low half.
 template <bool F16>
 __device__ __forceinline__ uint32_t pack_elem2(float lo, float hi) {
@@ -138,6 +134,22 @@ __device__ __forceinline__ uint32_t pack_elem2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&h);
   }
   return pack_bf16x2(lo, hi);
+}
+
+constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 16 bytes to shared memory, zeros where there are none.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t s, const void* g, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s), "l"(g), "r"(valid ? 16 : 0) : "memory");
+}
+// p / z for 0 <= p < 2^63 and z > 0; in 32 bits where both fit.
+__device__ __forceinline__ long long divide(long long p, long long z) {
+  if ((((unsigned long long)p | (unsigned long long)z) >> 32) == 0) return (uint32_t)p / (uint32_t)z;
+  return (long long)((unsigned long long)p / (unsigned long long)z);
 }
 
 }  // namespace spear
