@@ -354,7 +354,8 @@ spear_status spear_attn_decode(const spear_kv_cache* cache, const spear_kv_seqs*
  * the rows [starts[b], starts[b + 1]) of q and out (starts as for
  * spear_kv_append), token starts[b] + i at position seq_lens - (starts[b + 1]
  * - starts[b]) + i.  The new tokens' own K and V are in the cache already
- * (spear_kv_append on the same stream).  The workspace needs no zeroing.
+ * (spear_kv_append on the same stream).  Rows of out and lse that no sequence
+ * covers are not written.  The workspace needs no zeroing.
  */
 spear_status spear_attn_prefill_workspace_bytes(const spear_kv_cache* cache, int num_seqs, int num_tokens,
                                                 int num_q_heads, size_t* bytes);

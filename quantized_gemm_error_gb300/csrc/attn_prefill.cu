@@ -34,12 +34,14 @@
 // elements and mark the item; its rows add them back one by one at the end,
 // those that see them.
 //
-// Bound by the tensor cores and the power limit with heads of 128: one prompt
-// of 8192 tokens, 32 heads, takes 414 us, 1.33 PFLOP/s, in a short run and
-// 440 us once the clocks have fallen; 512 tokens over 32000, 64 heads on 8,
-// 370 and 420 us (1.46 and 1.29 PFLOP/s).  Bound by the softmax's latency with
-// heads of 64: four prompts of 2000 to 4096, window 1023, 172 us.  Small batches by
-// the first loads and the second kernel: three short chunks, 61 MB, 25 us.
+// Heads of 128: one prompt of 8192 tokens, 32 heads, takes 437 us, 1.26 PFLOP/s,
+// and 512 tokens over 32000, 64 heads on 8, 422 us, 1.28 PFLOP/s, at the power
+// limit (414 and 370 us in short runs, before the clocks fall).  The tensor
+// cores multiply in two thirds of the clocks; in the others both tiles' products
+// wait for a softmax (2900 clocks a pair of tiles, of which 2048 are MMAs).
+// Bound by the softmax's latency with heads of 64: four prompts of 2000 to 4096,
+// window 1023, 174 us.  Small batches by the first loads and the second kernel:
+// three short chunks, 61 MB, 25 us.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -1293,7 +1295,9 @@ bool q_boxes(const spear_attn& a, int group, int tokens) {
 // 3000 to 4096) and for sequences of few rows a K/V head (33 ragged chunks of
 // up to 1024 rows 540 against 581, three short ones 25.2 against 26.3), not for
 // those of many (4096 over 32000 keys 427 against 384, over 2000 268 against
-// 260; but 33 ragged ones of up to 8192 826 against 870).
+// 260).  The host knows the batch's average only, so the rule loses where a
+// batch of very ragged sequences is above it: 33 of up to 8192 rows take 870
+// gathered and would take 826 in boxes.
 int box_slots(const spear_kv_cache& c, long long rows) {
   if ((c.slot_stride <= 0 && c.page_size > 1) || (c.head_stride <= 0 && c.num_kv_heads > 1) ||
       (c.page_stride <= 0 && c.num_pages > 1) || std::max({c.slot_stride, c.head_stride, c.page_stride}) >= 1ll << 38)
