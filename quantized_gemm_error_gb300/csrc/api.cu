@@ -564,6 +564,6 @@ const char* spear_status_string(int status) {
 
 const char* spear_last_error(void) { return t_last_error; }
 
-const char* spear_version(void) { return "0.2.0"; }
+const char* spear_version(void) { return "0.3.0"; }
 
 }  // extern "C"
