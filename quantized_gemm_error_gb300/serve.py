@@ -130,6 +130,11 @@ class PagedServer:
     def __init__(self, blocks: Sequence[AttentionBlock], num_pages: int, page_size: int, max_seqs: int, max_pages: int,
                  device, stream: Optional[torch.cuda.Stream] = None):
         self.blocks: List[AttentionBlock] = list(blocks)
+        for i, b in enumerate(self.blocks):
+            if b.q.N % b.head_dim or b.k.N % b.head_dim or b.v.N != b.k.N or b.o.K != b.q.N or b.q_heads % b.kv_heads \
+                    or not b.q.K == b.k.K == b.v.K == self.blocks[0].q.K:
+                sizes = {n: (l.K, l.N) for n, l in (("q", b.q), ("k", b.k), ("v", b.v), ("o", b.o))}
+                raise ValueError(f"block {i}: heads of {b.head_dim} do not go with linears of (in, out) {sizes}")
         self.device, self.stream = torch.device(device), stream
         with self._on_stream():
             self.caches = [spear.new_kv_cache(num_pages, page_size, b.kv_heads, b.head_dim, device) for b in self.blocks]
@@ -168,7 +173,12 @@ class PagedServer:
             starts.append(starts[-1] + n)
         if starts[-1] != x.shape[0]:
             raise ValueError(f"x has {x.shape[0]} rows, counts add up to {starts[-1]}")
-        self.count.reserve(rows, counts)
+        width = self.blocks[0].q.K if self.blocks else None
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.get_device() != self.pool.index or width not in (None, x.shape[1]) \
+                or not x.is_contiguous():
+            raise ValueError(f"x must be a contiguous bfloat16 [tokens][{width}] tensor on {self.pool.device}, got {x.dtype} "
+                             f"{tuple(x.shape)} on {x.device}")
+        self.count.reserve(rows, counts)                     # (the last check: from here on the tokens count)
         here = torch.cuda.current_stream(self.device)
         with self._on_stream():
             outs = self._step(x, rows, counts, starts)
