@@ -9,7 +9,8 @@ the prefill kernels), and sequences can be forked, finished and the pool
 compacted between steps.  Everything runs in stream order on the GPU; no call
 reads an answer back.  A call that the pool would refuse is refused on the host
 before anything is launched (PoolFull where pages are short): the server counts
-along, so the pool's bookkeeping goes through its methods only.
+along.  Where the pool's bookkeeping was changed other than by its methods (a
+saved state put back, say), recount() has to follow.
 
 Norms, rotary embeddings and the feed-forward half are not part of it: a block
 maps its input rows to the o projection's output rows.
@@ -56,9 +57,19 @@ class PageCount:
     A row's pages are a list of runs [pages, rows that share them]; a run with more than one row is of whole pages."""
 
     def __init__(self, num_pages: int, page_size: int, max_seqs: int, max_pages: int):
-        self.page_size, self.max_pages, self.free_pages = page_size, max_pages, num_pages
+        self.page_size, self.max_pages, self.num_pages, self.free_pages = page_size, max_pages, num_pages, num_pages
         self.lens = [0] * max_seqs
         self.runs: List[list] = [[] for _ in range(max_seqs)]
+
+    def recount(self, lens: Sequence[int], table: Sequence[Sequence[int]]) -> None:
+        """Takes over a pool's lengths and block table."""
+        runs = {}                                            # by page: a run of its own
+        self.lens, self.runs = list(lens), []
+        for n, row in zip(lens, table):
+            self.runs.append([runs.setdefault(p, [1, 0]) for p in row[:-(-n // self.page_size)]])
+            for run in self.runs[-1]:
+                run[1] += 1
+        self.free_pages = self.num_pages - len(runs)
 
     def _check_rows(self, rows: Sequence[int], once: bool) -> None:
         if any(not 0 <= r < len(self.lens) for r in rows):
@@ -174,10 +185,10 @@ class PagedServer:
         if starts[-1] != x.shape[0]:
             raise ValueError(f"x has {x.shape[0]} rows, counts add up to {starts[-1]}")
         width = self.blocks[0].q.K if self.blocks else None
-        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.get_device() != self.pool.index or width not in (None, x.shape[1]) \
-                or not x.is_contiguous():
-            raise ValueError(f"x must be a contiguous bfloat16 [tokens][{width}] tensor on {self.pool.device}, got {x.dtype} "
-                             f"{tuple(x.shape)} on {x.device}")
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or width not in (None, x.shape[1]) or not x.is_contiguous() \
+                or x.get_device() != self.pool.index:
+            raise ValueError(f"x must be a contiguous bfloat16 [tokens][{width}] tensor on {self.pool.device}, "
+                             f"got {x.dtype} {tuple(x.shape)} on {x.device}")
         self.count.reserve(rows, counts)                     # (the last check: from here on the tokens count)
         here = torch.cuda.current_stream(self.device)
         with self._on_stream():
@@ -219,6 +230,11 @@ class PagedServer:
         self.count.free(rows)
         with self._on_stream():
             spear.spear_kv_free(self.pool, *self._rows(rows))
+
+    def recount(self) -> None:
+        """Counts the pool's pages anew, after a change to it that was not made by these methods.  Waits for the GPU."""
+        with self._on_stream():
+            self.count.recount(self.pool.seq_lens.tolist(), self.pool.block_table.tolist())
 
     def compact(self) -> None:
         """Moves the live pages to the front of the pool."""

@@ -42,3 +42,30 @@ def test_blocks_that_do_not_fit():
             PagedServer([_block(), _block(**bad)], 8, 16, 4, 4, "cuda")
     with pytest.raises(ValueError, match="block 1"):
         PagedServer([_block(), _block(width=1024)], 8, 16, 4, 4, "cuda")
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_a_pool_changed_from_outside_is_counted_anew(side):
+    from quantized_gemm_error_gb300 import spear
+    from quantized_gemm_error_gb300.serve import PagedServer, PoolFull
+    s = PagedServer([_block()], 4, 16, 4, 4, "cuda", torch.cuda.Stream() if side else None)
+    x = torch.ones(64, 512, dtype=BF16, device="cuda")
+    s.step(x[:40], [0], [40])
+    torch.cuda.synchronize()
+    saved = s.pool.snapshot()
+    s.step(x[:16], [1], [16])
+    torch.cuda.synchronize()
+    s.pool.restore(saved)                                    # the last step taken back
+    torch.cuda.synchronize()
+    with pytest.raises(PoolFull):
+        s.step(x[:16], [2], [16])
+    s.recount()
+    assert s.count.lens == [40, 0, 0, 0] and s.count.free_pages == 1
+    s.fork([0], [1])
+    with pytest.raises(PoolFull):
+        s.step(x[:9], [1], [9])
+    s.step(x[:8], [1], [8])
+    torch.cuda.synchronize()
+    assert spear.spear_get_device_status() == 0
+    assert s.pool.seq_lens.tolist() == s.count.lens == [40, 48, 0, 0]
+    assert s.pool.refs.tolist() == [2, 2, 1, 1] and s.count.free_pages == 0

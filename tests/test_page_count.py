@@ -60,3 +60,35 @@ def test_refusals_change_nothing():
     with pytest.raises(ValueError):
         c.free([0, 4])
     assert state() == before
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_recount_takes_over_a_pools_state(seed):
+    """A count made anew from lengths and table goes on like the one that was there all along."""
+    rng = random.Random(seed)
+    P, page, rows, cols = 60, 4, 8, 12
+    model, count = Model(P, page, rows, cols), PageCount(P, page, rows, cols)
+    for step in range(200):
+        if step % 5 == 4:
+            count = PageCount(P, page, rows, cols)
+            count.recount(model.lens, [r + [-1] * (cols - len(r)) for r in model.table])
+            assert count.lens == model.lens and count.free_pages == len(model.free_list())
+        op = rng.choice(["reserve", "reserve", "fork", "free", "compact"])
+        r = rng.sample(range(rows), 2)
+        if op == "reserve":
+            t = [rng.randint(0, 9) for _ in r]
+            ok, call = model.reserve(r, t), lambda: count.reserve(r, t)
+        elif op == "fork":
+            ok, call = model.fork(r[:1], r[1:]) is not None, lambda: count.fork(r[:1], r[1:])
+        elif op == "free":
+            model.free(r[:1])
+            ok, call = True, lambda: count.free(r[:1])
+        else:
+            model.compact()
+            continue
+        if ok:
+            call()
+        else:
+            with pytest.raises((ValueError, PoolFull)):
+                call()
+        assert count.lens == model.lens and count.free_pages == len(model.free_list())
